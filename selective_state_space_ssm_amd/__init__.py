@@ -420,9 +420,10 @@ def ssm_model_decode_step(desc, emb, layers, tokens, h, conv_state, logits=None,
 # --------------------------------------------------- training operators
 # These calls run on the device of their tensors, whichever device is current;
 # `stream` (default: that device's current stream) must belong to it.  What a
-# call allocates itself (outputs not passed in, a workspace) is safe on any
-# stream.  A call on a small tensor is all host time, so the checks are plain
-# comparisons in a row.
+# call allocates itself (outputs not passed in, a workspace) is allocated on the
+# stream it runs on: memory that was freed on the current stream may still be
+# written by work queued there.  A call on a small tensor is all host time, so
+# the checks are plain comparisons in a row.
 def _bad(t, dev, dtype, shape, name):
     """Raises for a tensor that is not one of `shape`, `dtype` on `dev`."""
     if not isinstance(t, torch.Tensor):
@@ -511,17 +512,20 @@ def _on_stream(dev, stream):
     return int(stream)
 
 
-def _made(dev, stream, *tensors):
-    """Tells torch's allocator of tensors made by a call that runs on a stream
-    other than the current one."""
-    if stream is None:
-        return
+def _new(shape, dtype, dev, stream, handle, returned=True):
+    """An uninitialised tensor for a call on `stream`, whose handle is `handle`,
+    from that stream's own memory.  A returned one is the caller's on the
+    current stream too, so its memory is not used again before both are done."""
+    if stream is None or handle == _current_stream(dev.index):
+        return torch.empty(shape, dtype=dtype, device=dev)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
-    if stream != torch.cuda.current_stream(dev):
-        for t in tensors:
-            if t is not None and t.numel():
-                t.record_stream(stream)
+        stream = torch.cuda.ExternalStream(handle, device=dev)
+    here = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    if returned and t.numel():
+        t.record_stream(here)
+    return t
 
 
 def _given_workspace(ws, dev):
@@ -539,9 +543,9 @@ def ssm_layer_norm_fwd(x, weight=None, bias=None, residual=None, residual_out=No
     dev, t, io, shape, T = _io_rows(x, "x")
     rows, vec, f32 = shape[:-1], shape[-1:], torch.float32
     with _on(dev):
-        made = None
+        handle = _on_stream(dev, stream)
         if y is None:
-            y = made = torch.empty(shape, dtype=t, device=dev)
+            y = _new(shape, t, dev, stream, handle)
         px, sx = _rows_ptr(x, dev, t, shape, "x")
         pr, sr = _rows_ptr(residual, dev, t, shape, "residual")
         po, so = _rows_ptr(residual_out, dev, t, shape, "residual_out")
@@ -549,8 +553,7 @@ def ssm_layer_norm_fwd(x, weight=None, bias=None, residual=None, residual_out=No
         desc = ssm_norm_desc(T, shape[-1], sx, sr, so, sy, io, eps)
         _check("ssm_layer_norm_fwd", lib().ssm_layer_norm_fwd(
             desc, px, pr, _dev_ptr(weight, dev, f32, vec, "weight"), _dev_ptr(bias, dev, f32, vec, "bias"), po, py,
-            _dev_ptr(mean, dev, f32, rows, "mean"), _dev_ptr(rstd, dev, f32, rows, "rstd"), _on_stream(dev, stream)))
-        _made(dev, stream, made)
+            _dev_ptr(mean, dev, f32, rows, "mean"), _dev_ptr(rstd, dev, f32, rows, "rstd"), handle))
     return y
 
 
@@ -572,29 +575,26 @@ def ssm_layer_norm_bwd(x, dy, mean, rstd, weight=None, dresidual=None, want=("dx
         if k not in ("dx", "dweight", "dbias"):
             raise ValueError("no gradient %r" % (k,))
     with _on(dev):
-        made = []
+        handle = _on_stream(dev, stream)
         for k in want:
             if k not in ("dx", "dweight", "dbias"):
                 raise ValueError("no gradient %r" % (k,))
             if k not in out:
-                out[k] = torch.empty(shape if k == "dx" else vec, dtype=t if k == "dx" else f32, device=dev)
-                made.append(out[k])
+                out[k] = _new(shape if k == "dx" else vec, t if k == "dx" else f32, dev, stream, handle)
         px, sx = _rows_ptr(x, dev, t, shape, "x")
         pdy, sdy = _rows_ptr(dy, dev, t, shape, "dy")
         pr, sr = _rows_ptr(dresidual, dev, t, shape, "dresidual")
         pdx, sdx = _rows_ptr(out.get("dx"), dev, t, shape, "dx")
         desc = ssm_norm_desc(T, shape[-1], sx, sr, sdx, sdy, io, 1.0)
         if workspace is None:
-            workspace = torch.empty(ssm_layer_norm_bwd_workspace_size(desc), dtype=torch.uint8, device=dev)
-            made.append(workspace)
+            workspace = _new(ssm_layer_norm_bwd_workspace_size(desc), torch.uint8, dev, stream, handle, returned=False)
         else:
             _given_workspace(workspace, dev)
         _check("ssm_layer_norm_bwd", lib().ssm_layer_norm_bwd(
             desc, px, _dev_ptr(weight, dev, f32, vec, "weight"), _dev_ptr(mean, dev, f32, rows, "mean"),
             _dev_ptr(rstd, dev, f32, rows, "rstd"), pdy, pr, pdx, _dev_ptr(out.get("dweight"), dev, f32, vec, "dweight"),
             _dev_ptr(out.get("dbias"), dev, f32, vec, "dbias"), workspace.data_ptr(), workspace.numel(),
-            _on_stream(dev, stream)))
-        _made(dev, stream, *made)
+            handle))
     return out
 
 
@@ -606,15 +606,14 @@ def ssm_token_logp_fwd(logits, targets, stats=None, logp=None, stream=None):
     dev, t, io, shape, T = _io_rows(logits, "logits")
     rows, f32 = shape[:-1], torch.float32
     with _on(dev):
-        made = None
+        handle = _on_stream(dev, stream)
         if logp is None:
-            logp = made = torch.empty(rows, dtype=f32, device=dev)
+            logp = _new(rows, f32, dev, stream, handle)
         pz, sz = _rows_ptr(logits, dev, t, shape, "logits")
         desc = ssm_logp_desc(T, shape[-1], sz, 0, io, 0)
         _check("ssm_token_logp_fwd", lib().ssm_token_logp_fwd(
             desc, pz, _dev_ptr(targets, dev, torch.int32, rows, "targets"), _dev_ptr(logp, dev, f32, rows, "logp"),
-            _dev_ptr(stats, dev, f32, rows + (2,), "stats"), _on_stream(dev, stream)))
-        _made(dev, stream, made)
+            _dev_ptr(stats, dev, f32, rows + (2,), "stats"), handle))
     return logp
 
 
@@ -624,17 +623,16 @@ def ssm_token_logp_bwd(logits, targets, stats, dlogp, dlogits=None, stream=None)
     dev, t, io, shape, T = _io_rows(logits, "logits")
     rows, f32 = shape[:-1], torch.float32
     with _on(dev):
-        made = None
+        handle = _on_stream(dev, stream)
         if dlogits is None:
-            dlogits = made = torch.empty(shape, dtype=t, device=dev)
+            dlogits = _new(shape, t, dev, stream, handle)
         pz, sz = _rows_ptr(logits, dev, t, shape, "logits")
         pd, sd = _rows_ptr(dlogits, dev, t, shape, "dlogits")
         desc = ssm_logp_desc(T, shape[-1], sz, sd, io, 0)
         _check("ssm_token_logp_bwd", lib().ssm_token_logp_bwd(
             desc, pz, _dev_ptr(targets, dev, torch.int32, rows, "targets"),
             _dev_ptr(stats, dev, f32, rows + (2,), "stats"), _dev_ptr(dlogp, dev, f32, rows, "dlogp"), pd,
-            _on_stream(dev, stream)))
-        _made(dev, stream, made)
+            handle))
     return dlogits
 
 
@@ -656,14 +654,14 @@ def ssm_policy_loss(logits, targets, old_logp, advantages, ref_logp=None, weight
     dev, t, io, shape, T = _io_rows(logits, "logits")
     rows, f32 = shape[:-1], torch.float32
     with _on(dev):
-        mloss = mws = None
+        handle = _on_stream(dev, stream)
         if loss is None:
-            loss = mloss = torch.empty(4, dtype=f32, device=dev)
+            loss = _new(4, f32, dev, stream, handle)
         pz, sz = _rows_ptr(logits, dev, t, shape, "logits")
         pd, sd = _rows_ptr(dlogits, dev, t, shape, "dlogits")
         desc = ssm_policy_desc(T, shape[-1], sz, sd, clip_low, clip_high, kl_beta, grad_scale, io, reduction)
         if workspace is None:
-            workspace = mws = torch.empty(ssm_policy_loss_workspace_size(desc), dtype=torch.uint8, device=dev)
+            workspace = _new(ssm_policy_loss_workspace_size(desc), torch.uint8, dev, stream, handle, returned=False)
         else:
             _given_workspace(workspace, dev)
         _check("ssm_policy_loss", lib().ssm_policy_loss(
@@ -671,8 +669,7 @@ def ssm_policy_loss(logits, targets, old_logp, advantages, ref_logp=None, weight
             _dev_ptr(old_logp, dev, f32, rows, "old_logp"), _dev_ptr(ref_logp, dev, f32, rows, "ref_logp"),
             _dev_ptr(advantages, dev, f32, rows, "advantages"), _dev_ptr(weights, dev, f32, rows, "weights"),
             _dev_ptr(loss, dev, f32, (4,), "loss"), _dev_ptr(logp, dev, f32, rows, "logp"), pd,
-            workspace.data_ptr(), workspace.numel(), _on_stream(dev, stream)))
-        _made(dev, stream, mloss, mws)
+            workspace.data_ptr(), workspace.numel(), handle))
     return loss
 
 
@@ -721,15 +718,14 @@ def ssm_clip_grad_norm(grads, max_norm, norm=None, workspace=None, stream=None):
         raise TypeError("grads must be a GradList")
     dev = grads.device
     with _on(dev):
-        mnorm = mws = None
+        handle = _on_stream(dev, stream)
         if norm is None:
-            norm = mnorm = torch.empty(2, dtype=torch.float32, device=dev)
+            norm = _new(2, torch.float32, dev, stream, handle)
         if workspace is None:
-            workspace = mws = torch.empty(grads.workspace_size, dtype=torch.uint8, device=dev)
+            workspace = _new(grads.workspace_size, torch.uint8, dev, stream, handle, returned=False)
         else:
             _given_workspace(workspace, dev)
         _check("ssm_clip_grad_norm", lib().ssm_clip_grad_norm(
             grads.array, len(grads.grads), max_norm, _dev_ptr(norm, dev, torch.float32, (2,), "norm"),
-            workspace.data_ptr(), workspace.numel(), _on_stream(dev, stream)))
-        _made(dev, stream, mnorm, mws)
+            workspace.data_ptr(), workspace.numel(), handle))
     return norm

@@ -1,0 +1,138 @@
+"""Where the training operators' binding allocates and what it passes on, on a
+machine without a GPU: tensors with made-up addresses, a library that only
+notes its calls, and streams that are plain names."""
+import contextlib
+import ctypes
+
+import pytest
+import torch
+
+import selective_state_space_ssm_amd as ssm
+
+HERE, THERE = 0x51, 0x52       # handles of the current stream and of the call's
+
+
+class Fake(torch.Tensor):
+    """A tensor on cuda:0 without memory."""
+    @staticmethod
+    def __new__(cls, shape, dtype=torch.float32, at=0x10000000, made_on=None):
+        t = torch.Tensor._make_wrapper_subclass(cls, shape, dtype=dtype, device="cuda:0")
+        t.at, t.made_on, t.recorded = at, made_on, []
+        return t
+
+    def data_ptr(self):
+        return self.at
+
+    def record_stream(self, stream):
+        self.recorded.append(stream)
+
+    @classmethod
+    def __torch_dispatch__(cls, func, types, args=(), kwargs=None):
+        raise NotImplementedError(func)
+
+
+class Stream:
+    """Stands for torch.cuda.Stream and ExternalStream."""
+    device = torch.device("cuda:0")
+
+    def __init__(self, handle, device=None):
+        self.cuda_stream = handle
+
+    def __eq__(self, other):
+        return self.cuda_stream == other.cuda_stream
+
+
+class Library:
+    """Notes the entry points called; the size queries answer 64 bytes."""
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            if name.endswith("_size"):
+                out = args[-1]
+                (out._obj if hasattr(out, "_obj") else out).value = 64
+            else:
+                self.calls.append((name, args))
+            return 0
+        return call
+
+
+@pytest.fixture
+def world(monkeypatch):
+    """.made: what was allocated; .lib: what was called."""
+    class World:
+        made, now, lib = [], HERE, Library()
+
+    w = World()
+    w.made = []
+
+    @contextlib.contextmanager
+    def on_stream(stream):
+        w.now, before = stream.cuda_stream, w.now
+        yield
+        w.now = before
+
+    def empty(*shape, dtype=torch.float32, device=None):
+        shape = shape[0] if len(shape) == 1 and not isinstance(shape[0], int) else shape
+        t = Fake(tuple(shape), dtype, 0x20000000 + 0x100000 * len(w.made), w.now)
+        w.made.append(t)
+        return t
+
+    monkeypatch.setattr(ssm, "lib", lambda: w.lib)
+    monkeypatch.setattr(ssm, "_current_device", lambda: 0)
+    monkeypatch.setattr(ssm, "_current_stream", lambda i: w.now)
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: Stream(w.now))
+    monkeypatch.setattr(torch.cuda, "stream", on_stream)
+    monkeypatch.setattr(torch, "empty", empty)
+    return w
+
+
+def _calls():
+    x, v, t = Fake((8, 16)), Fake((8,)), Fake((8,), torch.int32)
+    grads = ssm.GradList([Fake((40,)), Fake((3, 4), torch.bfloat16)])
+    return {
+        "ssm_layer_norm_fwd": lambda s: [ssm.ssm_layer_norm_fwd(x, stream=s)],
+        "ssm_layer_norm_bwd": lambda s: list(ssm.ssm_layer_norm_bwd(x, x, v, v, stream=s).values()),
+        "ssm_token_logp_fwd": lambda s: [ssm.ssm_token_logp_fwd(x, t, stream=s)],
+        "ssm_token_logp_bwd": lambda s: [ssm.ssm_token_logp_bwd(x, t, Fake((8, 2)), v, stream=s)],
+        "ssm_policy_loss": lambda s: [ssm.ssm_policy_loss(x, t, v, v, stream=s)],
+        "ssm_clip_grad_norm": lambda s: [ssm.ssm_clip_grad_norm(grads, 1.0, stream=s)],
+    }
+
+
+CALLS = ["ssm_layer_norm_fwd", "ssm_layer_norm_bwd", "ssm_token_logp_fwd", "ssm_token_logp_bwd", "ssm_policy_loss",
+         "ssm_clip_grad_norm"]
+
+
+@pytest.mark.parametrize("how", ["stream", "handle"])
+@pytest.mark.parametrize("name", CALLS)
+def test_a_call_allocates_on_the_stream_it_runs_on(name, how, world):
+    """Memory freed on the current stream may still be written by work queued
+    there, so nothing that the call's own stream uses may come from it."""
+    out = _calls()[name](Stream(THERE) if how == "stream" else THERE)
+    (called, args), = world.lib.calls
+    assert called == name and args[-1] == THERE and world.now == HERE
+    assert world.made and all(t.made_on == THERE for t in world.made)
+    for t in world.made:       # what the caller receives is used on the current stream too
+        assert t.recorded == ([Stream(HERE)] if any(t is o for o in out) else [])
+
+
+@pytest.mark.parametrize("how", [None, "stream", "handle"])
+@pytest.mark.parametrize("name", CALLS)
+def test_on_the_current_stream_nothing_is_recorded(name, how, world):
+    _calls()[name]({None: None, "stream": Stream(HERE), "handle": HERE}[how])
+    (called, args), = world.lib.calls
+    assert called == name and args[-1] == HERE
+    assert world.made and all(t.made_on == HERE and not t.recorded for t in world.made)
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_a_stream_of_another_device_is_refused(name, world):
+    other = Stream(THERE)
+    other.device = torch.device("cuda:1")
+    with pytest.raises(ValueError):
+        _calls()[name](other)
+    assert not world.lib.calls
