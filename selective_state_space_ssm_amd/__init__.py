@@ -4,7 +4,8 @@ A thin ctypes layer over the C ABI declared in include/ssm.h: every function
 here has the name of the C entry point it calls and only marshals arguments
 (torch tensors -> device pointers, the current HIP stream, descriptors).
 PyTorch supplies device memory and streams; all arithmetic runs in the HIP
-kernels.  Outputs that are not passed in are allocated with torch.empty.
+kernels.  Outputs that are not passed in are allocated with torch.empty, on the
+stream that the call runs on.
 
 The library must have been built (selective_state_space_ssm_amd/build.py);
 importing the binding never falls back to any other implementation.
@@ -207,6 +208,13 @@ def _stream(stream):
     return ctypes.c_void_p(int(stream))
 
 
+def _alloc(shape, dtype, device, stream, returned=True):
+    """What a call on `stream` allocates itself: from that stream's memory."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _new(shape, dtype, device, stream, _stream(stream).value or 0, returned)
+
+
 def _check(fn, rc):
     if rc != SSM_OK:
         raise SSMError(fn, rc)
@@ -224,7 +232,7 @@ def conv1d_causal(x, w, b=None, state_in=None, state_out=None, y=None, silu=True
     W = w.shape[1]
     io = _io_code(x)
     if y is None:
-        y = torch.empty_like(x)
+        y = _alloc(x.shape, x.dtype, x.device, stream)
     desc = ssm_conv_desc(Bn, L, D, W, 1 if silu else 0, io, 0)
     _check("conv1d_causal", lib().conv1d_causal(
         ctypes.byref(desc), _ptr(x, x.dtype, "x"), _f32(w, "w"), _f32(b, "b"),
@@ -250,12 +258,12 @@ def ssm_scan_bwd_workspace_size(desc) -> int:
     return int(n.value)
 
 
-def _workspace(nbytes, given, device):
+def _workspace(nbytes, given, device, stream):
     if nbytes == 0:
         return given
     if given is not None:
         return given
-    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return _alloc(nbytes, torch.uint8, device, stream, returned=False)
 
 
 def ssm_scan_fwd(x, dt_raw, A_log, B, C, dt_bias=None, Dskip=None, z=None, conv_w=None, conv_b=None,
@@ -267,8 +275,8 @@ def ssm_scan_fwd(x, dt_raw, A_log, B, C, dt_bias=None, Dskip=None, z=None, conv_
     W = conv_w.shape[1] if conv_w is not None else 0
     desc = _scan_desc(x, N, W, disc, chunk_len)
     if y is None:
-        y = torch.empty_like(x)
-    ws = _workspace(ssm_scan_fwd_workspace_size(desc), workspace, x.device)
+        y = _alloc(x.shape, x.dtype, x.device, stream)
+    ws = _workspace(ssm_scan_fwd_workspace_size(desc), workspace, x.device, stream)
     t = x.dtype
     _check("ssm_scan_fwd", lib().ssm_scan_fwd(
         ctypes.byref(desc), _ptr(x, t, "x"), _ptr(dt_raw, t, "dt_raw"), _f32(dt_bias, "dt_bias"),
@@ -291,7 +299,7 @@ def ssm_scan_fwd_static(x, dt_raw, A_log, B, C, dt_bias=None, Dskip=None, z=None
     W = conv_w.shape[1] if conv_w is not None else 0
     desc = _scan_desc(x, N, W, disc, chunk_len)
     if y is None:
-        y = torch.empty_like(x)
+        y = _alloc(x.shape, x.dtype, x.device, stream)
     t = x.dtype
     _check("ssm_scan_fwd_static", lib().ssm_scan_fwd_static(
         ctypes.byref(desc), _ptr(x, t, "x"), _ptr(dt_raw, t, "dt_raw"), _f32(dt_bias, "dt_bias"),
@@ -332,8 +340,8 @@ def ssm_scan_bwd(x, dt_raw, A_log, B, C, dy, dt_bias=None, Dskip=None, z=None, c
             continue
         if k not in out:
             shp, dt_ = shapes[k]
-            out[k] = torch.empty(shp, dtype=dt_, device=x.device)
-    ws = _workspace(ssm_scan_bwd_workspace_size(desc), workspace, x.device)
+            out[k] = _alloc(shp, dt_, x.device, stream)
+    ws = _workspace(ssm_scan_bwd_workspace_size(desc), workspace, x.device, stream)
     g = out.get
     _check("ssm_scan_bwd", lib().ssm_scan_bwd(
         ctypes.byref(desc), _ptr(x, t, "x"), _ptr(dt_raw, t, "dt_raw"), _f32(dt_bias, "dt_bias"),
@@ -361,7 +369,7 @@ def ssm_step(h, x, dt_raw, A_log, B, C, conv_state=None, z=None, conv_w=None, co
         raise TypeError("h must be float32 or bfloat16, got %s" % h.dtype)
     desc = ssm_step_desc(K, S, D, N, W, _io_code(x), disc, _io_code(h))
     if y is None:
-        y = torch.empty_like(x)
+        y = _alloc(x.shape, x.dtype, x.device, stream)
     _check("ssm_step", lib().ssm_step(
         ctypes.byref(desc), _ptr(h, h.dtype, "h"), _f32(conv_state, "conv_state"), _ptr(x, t, "x"),
         _ptr(dt_raw, t, "dt_raw"), _ptr(B, t, "B"), _ptr(C, t, "C"), _ptr(z, t, "z"), _f32(conv_w, "conv_w"),
@@ -406,10 +414,10 @@ def ssm_model_decode_step(desc, emb, layers, tokens, h, conv_state, logits=None,
     Returns logits [S, vocab]."""
     S, V = desc.nstreams, desc.vocab
     if logits is None:
-        logits = torch.empty(S, V, device=tokens.device, dtype=torch.float32)
+        logits = _alloc((S, V), torch.float32, tokens.device, stream)
     ws = workspace
     if ws is None:
-        ws = torch.empty(ssm_model_decode_workspace_size(desc), dtype=torch.uint8, device=tokens.device)
+        ws = _alloc(ssm_model_decode_workspace_size(desc), torch.uint8, tokens.device, stream, returned=False)
     _check("ssm_model_decode_step", lib().ssm_model_decode_step(
         ctypes.byref(desc), _f32(emb, "emb"), _f32(norm_f_w, "norm_f_w"), _f32(norm_f_b, "norm_f_b"),
         layers.array, _ptr(tokens, torch.int32, "tokens"), _f32(h, "h"), _f32(conv_state, "conv_state"),

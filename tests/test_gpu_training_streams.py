@@ -101,3 +101,28 @@ def test_default_stream_by_its_handle_from_another():
         got = call(0)[0]
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("name", ["fwd", "bwd"])
+def test_scan_beside_work_queued_on_the_current_stream(name):
+    """The same for the scan and its backward, a time split with its workspace."""
+    g = _gen(2)
+    B, L, D, N = 2, 512, 64, 16
+    u, dt, dy = [_randn(g, B, L, D) for _ in range(3)]
+    Bm, Cm, A = _randn(g, B, L, N), _randn(g, B, L, N), _randn(g, D, N) * 0.1
+    calls = {"fwd": lambda s: [ssm.ssm_scan_fwd(u, dt, A, Bm, Cm, chunk_len=64, stream=s)],
+             "bwd": lambda s: list(ssm.ssm_scan_bwd(u, dt, A, Bm, Cm, dy, chunk_len=64, stream=s).values())}
+    want = [o.clone() for o in calls[name](None)]
+    s = torch.cuda.Stream()
+    a = torch.ones(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    for k in range(3):
+        for _ in range(4):
+            a = a @ a
+        late = [torch.full(o.shape, float("nan"), device="cuda") for o in want]
+        late += [torch.full((n // 4,), float("nan"), device="cuda") for n in (512, 4096, 1 << 16, 1 << 20, 1 << 22, 1 << 24)]
+        del late
+        got = calls[name](s)
+        torch.cuda.synchronize()
+        for o, w in zip(got, want):
+            assert torch.equal(o, w), k

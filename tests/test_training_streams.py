@@ -1,5 +1,5 @@
-"""Where the training operators' binding allocates and what it passes on, on a
-machine without a GPU: tensors with made-up addresses, a library that only
+"""Where the binding allocates and what it passes on, on a machine without a
+GPU: tensors with made-up addresses, a library that only
 notes its calls, and streams that are plain names."""
 import contextlib
 import ctypes
@@ -87,6 +87,7 @@ def world(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: Stream(w.now))
     monkeypatch.setattr(torch.cuda, "stream", on_stream)
     monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(torch, "empty_like", lambda t: empty(t.shape, dtype=t.dtype))
     return w
 
 
@@ -136,3 +137,45 @@ def test_a_stream_of_another_device_is_refused(name, world):
     with pytest.raises(ValueError):
         _calls()[name](other)
     assert not world.lib.calls
+
+
+def _scan_calls():
+    x, bc = Fake((2, 8, 16)), Fake((2, 8, 4))
+    vec, mat, w = Fake((16,)), Fake((16, 4)), Fake((16, 4))
+    desc = ssm.ssm_model_desc(3, 11, 8, 1, 16, 4, 2, 4, 0)
+    step = lambda *s: Fake((1, 3) + s)
+    layers = ssm.ModelLayers([{f: Fake((4,)) for f in ssm.LAYER_FIELDS}])
+    return {
+        "conv1d_causal": lambda s: [ssm.conv1d_causal(x, w, stream=s)],
+        "ssm_scan_fwd": lambda s: [ssm.ssm_scan_fwd(x, x, mat, bc, bc, stream=s)],
+        "ssm_scan_fwd_static": lambda s: [ssm.ssm_scan_fwd_static(x, x, mat, bc, bc, stream=s)],
+        "ssm_scan_bwd": lambda s: list(ssm.ssm_scan_bwd(x, x, mat, bc, bc, x, dt_bias=vec, Dskip=vec, z=x, conv_w=w,
+                                                        stream=s).values()),
+        "ssm_step": lambda s: [ssm.ssm_step(step(16, 4), step(16), step(16), Fake((1, 16, 4)), step(4), step(4),
+                                            stream=s)],
+        "ssm_model_decode_step": lambda s: [ssm.ssm_model_decode_step(
+            desc, Fake((11, 8)), layers, Fake((3,), torch.int32), step(16, 4), step(3, 16), stream=s)],
+    }
+
+
+SCANS = ["conv1d_causal", "ssm_scan_fwd", "ssm_scan_fwd_static", "ssm_scan_bwd", "ssm_step", "ssm_model_decode_step"]
+
+
+@pytest.mark.parametrize("how", ["stream", "handle"])
+@pytest.mark.parametrize("name", SCANS)
+def test_a_scan_call_allocates_on_the_stream_it_runs_on(name, how, world):
+    out = _scan_calls()[name](Stream(THERE) if how == "stream" else THERE)
+    (called, args), = world.lib.calls
+    assert called == name and args[-1].value == THERE and world.now == HERE
+    assert world.made and all(t.made_on == THERE for t in world.made)
+    for t in world.made:
+        assert t.recorded == ([Stream(HERE)] if any(t is o for o in out) else [])
+
+
+@pytest.mark.parametrize("how", [None, "stream", "handle"])
+@pytest.mark.parametrize("name", SCANS)
+def test_a_scan_call_on_the_current_stream_records_nothing(name, how, world):
+    _scan_calls()[name]({None: None, "stream": Stream(HERE), "handle": HERE}[how])
+    (called, args), = world.lib.calls
+    assert called == name and args[-1].value == HERE
+    assert world.made and all(t.made_on == HERE and not t.recorded for t in world.made)
