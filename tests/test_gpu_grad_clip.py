@@ -164,3 +164,24 @@ def test_offsets_past_32_bits():
     assert abs(norm[0].item() - math.sqrt(n)) <= 2 * U * math.sqrt(n)
     want = torch.tensor(norm[1].item()).to(B)
     assert (g[:5] == want.cuda()).all() and (g[-70000:] == want.cuda()).all() and (g[n // 2:n // 2 + 9] == want.cuda()).all()
+
+
+def test_a_kept_list_follows_replaced_memory():
+    """Gradients and outputs given new memory by `.data` and `set_` after the
+    list was built; the old memory stays as it was."""
+    g = _gen(7)
+    for in_place in (True, False):
+        grads = [_randn(g, n) for n in (100, 9000, 8)]
+        outs = None if in_place else [torch.empty(n, dtype=(F, B, F)[k], device="cuda") for k, n in enumerate((100, 9000, 8))]
+        h = ssm.GradList(grads, out=outs)
+        ssm.ssm_clip_grad_norm(h, 1e9)
+        old = grads[1].data
+        kept = old.clone()
+        grads[1].data = _randn(g, 9000)
+        grads[2].set_(_randn(g, 8))
+        if outs is not None:
+            outs[0].data = torch.full((100,), 9.0, device="cuda")
+        before = [t.clone() for t in grads]
+        norm = ssm.ssm_clip_grad_norm(h, 0.5)
+        _check(before, grads if in_place else outs, 0.5, norm)
+        assert torch.equal(old, kept)

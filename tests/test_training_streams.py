@@ -23,6 +23,9 @@ class Fake(torch.Tensor):
     def data_ptr(self):
         return self.at
 
+    def untyped_storage(self):
+        return "memory at %#x" % self.at
+
     def record_stream(self, stream):
         self.recorded.append(stream)
 
@@ -45,13 +48,14 @@ class Stream:
 class Library:
     """Notes the entry points called; the size queries answer 64 bytes."""
     def __init__(self):
-        self.calls = []
+        self.calls, self.sizes = [], 0
 
     def __getattr__(self, name):
         def call(*args):
             if name.endswith("_size"):
                 out = args[-1]
                 (out._obj if hasattr(out, "_obj") else out).value = 64
+                self.sizes += 1
             else:
                 self.calls.append((name, args))
             return 0
@@ -179,3 +183,42 @@ def test_a_scan_call_on_the_current_stream_records_nothing(name, how, world):
     (called, args), = world.lib.calls
     assert called == name and args[-1].value == HERE
     assert world.made and all(t.made_on == HERE and not t.recorded for t in world.made)
+
+
+def _addresses(args):
+    return [(args[0][i].grad, args[0][i].out) for i in range(args[1])]
+
+
+@pytest.mark.parametrize("which", ["grad", "out", "in place"])
+def test_a_gradient_list_follows_its_tensors(which, world):
+    """A tensor whose memory was replaced since the list was built: the call
+    takes its present address, not the old one, which may be another tensor's."""
+    g = [Fake((40,), at=0x1000), Fake((8,), at=0x2000), Fake((8,), at=0x3000)]
+    o = [Fake((40,), at=0x4000), None, Fake((8,), torch.bfloat16, at=0x5000)]
+    h = ssm.GradList(g) if which == "in place" else ssm.GradList(g, out=o)
+    ssm.ssm_clip_grad_norm(h, 1.0)
+    sizes = world.lib.sizes
+    ssm.ssm_clip_grad_norm(h, 1.0)
+    assert world.lib.sizes == sizes                         # nothing moved: the list is not built again
+    (o if which == "out" else g)[2].at = 0x9000
+    ssm.ssm_clip_grad_norm(h, 1.0)
+    first, second, third = [_addresses(a) for _, a in world.lib.calls]
+    assert first == second
+    want = {"in place": [(0x1000, 0x1000), (0x2000, 0x2000), (0x9000, 0x9000)],
+            "grad": [(0x1000, 0x4000), (0x2000, None), (0x9000, 0x5000)],
+            "out": [(0x1000, 0x4000), (0x2000, None), (0x3000, 0x9000)]}[which]
+    assert third == want
+
+
+def test_a_moved_gradient_is_checked_again(world):
+    class Strided(Fake):
+        def is_contiguous(self):
+            return self.at == 0x1000
+
+    g = Strided((40,), at=0x1000)
+    h = ssm.GradList([g])
+    g.at = 0x2000
+    for call in (lambda: ssm.ssm_clip_grad_norm(h, 1.0), lambda: ssm.ssm_clip_grad_norm_workspace_size(h), h.refresh):
+        with pytest.raises(ValueError):
+            call()
+    assert not world.lib.calls
