@@ -397,7 +397,7 @@ typedef struct ssm_norm_desc {
  *   mean = mean(s),  rstd = 1 / sqrt(mean((s - mean)^2) + eps)
  *   y = (s - mean) * rstd * weight + bias
  * s is normalised before it is rounded to io for residual_out.  Sums are
- * float32: rows reaching past 1e18 either way overflow their squares.
+ * float32: rows reaching past 1e18 either way may overflow their squares.
  *   x            io  [T, D]  required when T > 0
  *   residual     io  [T, D]  optional
  *   weight, bias f32 [D]     optional (1, 0)

@@ -169,16 +169,20 @@ __global__ __launch_bounds__(block_of(G)) void norm_fwd_kernel(NormFwdArgs a) {
     row_sums<G>(m, red[0], wv);
     const float mu = m[0] / (float)D;
     es = at.has_edge() ? es - mu : 0.0f;
-    float v[1] = {es * es};
+    // squares are added as parts of their mean: 2^e, the largest power of two that
+    // is at most 1 / D, changes no digit and keeps a wide row's sum of squares in
+    // float32 as far as its mean square is
+    const float part = __uint_as_float((uint32_t)(127 - (D > 1 ? 32 - __clz(D - 1) : 0)) << 23);
+    float v[1] = {(es * part) * es};
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int i = 0; i < VE; ++i) {
             s[k][i] = at.has(k) ? s[k][i] - mu : 0.0f;
-            v[0] = fmaf(s[k][i], s[k][i], v[0]);
+            v[0] = fmaf(s[k][i] * part, s[k][i], v[0]);
         }
     row_sums<G>(v, red[1], wv);
-    const float rs = 1.0f / sqrtf(v[0] / (float)D + a.eps);
+    const float rs = 1.0f / sqrtf(v[0] / ((float)D * part) + a.eps);
     if (!act) return;
 #pragma unroll
     for (int k = 0; k < NV; ++k)

@@ -421,3 +421,19 @@ def test_with_another_device_current(monkeypatch):
     assert torch.equal(ssm.ssm_layer_norm_bwd(x, x, *_stats(x))["dx"], out["dx"])
     assert torch.equal(ssm.ssm_policy_loss(z, t, lp, lp), loss)
     assert torch.equal(ssm.ssm_clip_grad_norm(ssm.GradList([out["dx"]]), math.inf)[:1], norm[:1])
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [1, 7, 341, 384, 2050, 8192, 16384])
+def test_rows_of_large_values(D, dt):
+    """Values up to the documented 1e18 either way, whose squares' sum over a
+    wide row float32 does not hold though their mean it does."""
+    g, t = _gen(D + 21), DT[dt]
+    sign = torch.where(torch.rand(4, D, generator=g, device="cuda") < 0.5, -1.0, 1.0)
+    x = (sign * torch.tensor([[1e17], [3e17], [5e17], [0.98e18]], device="cuda")).to(t)
+    r = torch.zeros_like(x)
+    w, b = _randn(g, D), _randn(g, D)
+    mean, rstd = torch.empty(4, device="cuda"), torch.empty(4, device="cuda")
+    s = torch.empty_like(x)
+    y = ssm.ssm_layer_norm_fwd(x, w, b, residual=r, residual_out=s, mean=mean, rstd=rstd, eps=1e-5)
+    _check_fwd(x, r, w, b, 1e-5, y, s, mean, rstd)
