@@ -575,3 +575,23 @@ def test_two_graphs_with_a_workspace_each():
             for a, b in zip(outs[i], want[i]):
                 assert torch.equal(a, b), (k, i)
         run(0)
+
+
+@pytest.mark.parametrize("T,V,dt", [(16384, 4096, "f32"), (16384, 4100, "bf16"), (4096, 50001, "bf16"), (2048, 70001, "f32")])
+def test_log_sums_are_off_to_either_side(T, V, dt):
+    """The mean signed error of log p over many rows.  With the largest logit as
+    the target log p is -log sum, between -8 and -1 here: its rounding to float32
+    (half a step 2.4e-7 at most, deviation 1.4e-7) and the row's own roundings
+    (deviation under 1e-7) average to 1.8e-7 / sqrt(2048) = 4e-9 over the fewest
+    rows; the hardware's 2^x is off by -3.3e-9 on the average (its own rounding,
+    measured over 2^24 arguments), which enters log sum as it is.  Four
+    deviations and that bias: 2e-8."""
+    g, t = _gen(T + V), DT[dt]
+    z = _randn(g, T, V, dtype=t, scale=2.5)
+    tgt = z.argmax(-1).int()
+    ref = torch.cat([_softmax_ref(z[i:i + 512], tgt[i:i + 512])[2] for i in range(0, T, 512)])
+    logp = torch.empty(T, device="cuda")
+    ssm.ssm_policy_loss(z, tgt, None, logp.new_zeros(T), logp=logp)
+    for got in (ssm.ssm_token_logp_fwd(z, tgt), logp):
+        assert -8 < ref.min() and ref.max() < 0
+        assert abs((got.double() - ref).mean().item()) < 2e-8
