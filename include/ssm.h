@@ -426,7 +426,8 @@ ssm_status ssm_layer_norm_bwd_workspace_size(const ssm_norm_desc *desc, size_t *
  *   weight     f32 [D]     optional (1)
  *   dx         io  [T, D]  optional output (may be exactly dy or exactly dresidual)
  *   dweight, dbias f32 [D] optional outputs (zeros when T = 0); the order of
- *                          their sums is fixed for a shape
+ *                          their sums is fixed for a shape: float32 over at
+ *                          most 512 rows and 16 such groups, 64-bit above
  *   workspace  ssm_layer_norm_bwd_workspace_size bytes (required)
  * x, mean, rstd and dy are required when T > 0.
  */

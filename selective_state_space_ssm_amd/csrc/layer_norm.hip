@@ -10,7 +10,8 @@
 // A row lives in the registers of the G lanes that share it (16 lanes to a
 // whole workgroup), as 16-byte vectors, so memory is read and written once;
 // the variance is the mean square of s - mu, taken from those registers (no
-// cancellation for rows far from zero).  Statistics and sums are float32.
+// cancellation for rows far from zero).  Statistics and sums are float32; the
+// parameters' sums are float32 over at most 512 rows and 64-bit above.
 // Bound by HBM bytes.  The backward's parameter sums stay in registers while
 // a workgroup walks its rows; one partial per workgroup goes to the
 // workspace, and a second launch adds the partials in a fixed order.
@@ -327,16 +328,17 @@ __global__ __launch_bounds__(block_of(G)) void norm_bwd_kernel(NormBwdArgs a) {
     }
 }
 
-// dw, db: the partials of every workgroup.  32 columns x 32 strips of
-// partials per workgroup (128-byte reads); strips added in order.
+// dw, db: the partials of every workgroup, added in 64 bits (there are as many as
+// the rows make).  32 columns x 32 strips of partials per workgroup (128-byte
+// reads); strips added in order.
 __global__ __launch_bounds__(1024) void norm_bwd_reduce(const float *ws, int64_t P, int64_t D, float *dw, float *db) {
-    __shared__ float part[32][33];
+    __shared__ double part[32][33];
     const int cl = threadIdx.x & 31, st = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + cl;
-    float t = 0.0f;
+    double t = 0.0;
     if (c < 2 * D) {
 #pragma unroll 8
-        for (int64_t p = st; p < P; p += 32) t += ws[p * 2 * D + c];
+        for (int64_t p = st; p < P; p += 32) t += (double)ws[p * 2 * D + c];
     }
     part[st][cl] = t;
     __syncthreads();
@@ -344,9 +346,9 @@ __global__ __launch_bounds__(1024) void norm_bwd_reduce(const float *ws, int64_t
 #pragma unroll
         for (int k = 1; k < 32; ++k) t += part[k][cl];
         if (c < D) {
-            if (dw) dw[c] = t;
+            if (dw) dw[c] = (float)t;
         } else if (db) {
-            db[c - D] = t;
+            db[c - D] = (float)t;
         }
     }
 }
@@ -369,11 +371,16 @@ constexpr int kBwdVecs = 2;
 // Workgroups of the backward: two per CU, one where a row takes 512 lanes or
 // more (a CU holds one of those; 19531 x 5120 bfloat16: 151 us, 167 with two),
 // fewer where the rows run out; one alone for rows that it takes in two goes (a
-// third costs what the launch of the sums does).
+// third costs what the launch of the sums does); more where a row group would add
+// more than kChain rows to its float32 parameter sums, whose error grows with them (as
+// many for each CU: 300001 x 4104 bfloat16 1519 us with 768 workgroups, 1872 with
+// the 586 that would do, 1481 with 256 that add 1172 rows each).
+constexpr int64_t kChain = 512;
 int64_t bwd_blocks(int64_t T, int64_t D, int bf16) {
     const int G = row_lanes(D / (bf16 ? kVec<bf16_t> : kVec<float>), kBwdVecs);
     const int64_t R = block_of(G) / G;
-    return T <= 2 * R ? 1 : std::min<int64_t>(G >= 512 ? 256 : 512, (T + R - 1) / R);
+    const int64_t resident = G >= 512 ? 256 : 512, most = resident * R * kChain;
+    return T <= 2 * R ? 1 : std::min((T + R - 1) / R, resident * ((T + most - 1) / most));
 }
 
 struct Fwd {

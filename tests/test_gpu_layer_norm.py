@@ -437,3 +437,18 @@ def test_rows_of_large_values(D, dt):
     s = torch.empty_like(x)
     y = ssm.ssm_layer_norm_fwd(x, w, b, residual=r, residual_out=s, mean=mean, rstd=rstd, eps=1e-5)
     _check_fwd(x, r, w, b, 1e-5, y, s, mean, rstd)
+
+
+@pytest.mark.parametrize("T,D,dt", [(1 << 27, 2, "f32"), (300_001, 4104, "bf16")])
+def test_parameter_sums_over_many_rows(T, D, dt):
+    """Equal terms, whose float32 sum is off to one side: at most 512 rows are
+    added in float32, then at most 16 such sums, then 64 bits: 530 half-steps
+    with the term's and the result's own, whatever the number of rows."""
+    t = DT[dt]
+    c = torch.tensor(1.1, dtype=t).item()
+    x, dy = torch.ones(T, D, dtype=t, device="cuda"), torch.full((T, D), c, dtype=t, device="cuda")
+    mean, rstd = torch.zeros(T, device="cuda"), torch.ones(T, device="cuda")
+    out = ssm.ssm_layer_norm_bwd(x, dy, mean, rstd, want=("dweight", "dbias"))
+    ref = torch.full((D,), T * c, dtype=torch.float64, device="cuda")
+    within(out["dbias"], ref, 530 * U * ref, "dbias")
+    within(out["dweight"], ref, 530 * U * ref, "dweight")
