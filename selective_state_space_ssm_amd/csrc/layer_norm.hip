@@ -208,8 +208,10 @@ __global__ __launch_bounds__(block_of(G)) void norm_bwd_kernel(NormBwdArgs a) {
     __shared__ float red[2][BLK / 64][2];
     const int wv = threadIdx.x >> 6, grp = R > 1 ? threadIdx.x / G : 0, D = (int)a.D;
     // 20000 x 4097 bfloat16: 142 us shifted, 174 not; 19996 x 5001: 193, 251; with
-    // 128 lanes other rows hide the odd loads, with 1024 it spills (11109 x 9001:
-    // 517 us not shifted, 578 shifted)
+    // 128 lanes other rows hide the odd loads.  With 1024 lanes there are 128 registers,
+    // and bfloat16 spills as it is (92 bytes a lane, 148 with an edge; float32 above
+    // 8192 values 20 to 196): 11110 x 9000 bfloat16 306 us against 157 for its bytes,
+    // 11109 x 9001 518, and 578 shifted
     using Row = RowOf<T, NV, G, EDGE, EDGE && sizeof(T) == 2 && (G == 256 || G == 512)>;
     const Row at(threadIdx.x % G, D);
     const float invD = 1.0f / (float)D;
@@ -369,7 +371,11 @@ template <typename T> constexpr int kFwdVecs = sizeof(T) == 4 ? 2 : 4;
 constexpr int kBwdVecs = 2;
 
 // Workgroups of the backward: two per CU, one where a row takes 512 lanes or
-// more (a CU holds one of those; 19531 x 5120 bfloat16: 151 us, 167 with two),
+// more.  In bfloat16 a CU holds one of those (162 and 182 registers; 19531 x 5120:
+// 151 us, 167 with two), in float32 two (88 and 100), but one with half the
+// partial sums is the faster from 4096 values on: with dresidual 16384 x 4096 190 us
+// against 206, 12000 x 5120 179 and 193, 8192 x 8192 205 and 212, 4096 x 16384 315
+// and 342 (20000 x 2560 165 and 165, without dresidual 139 and 118);
 // fewer where the rows run out; one alone for rows that it takes in two goes (a
 // third costs what the launch of the sums does); more where a row group would add
 // more than kChain rows to its float32 parameter sums, whose error grows with them (as
